@@ -291,7 +291,7 @@ WKV_API wkv_status diag_scan_bf16(int64_t B, int64_t T, int64_t D,
  * The state and every sum are fp32, whatever the I/O type.
  * `scratch`: caller's device memory, 16-byte aligned, at least
  * gated_delta_scratch() bytes (0 for single tokens, short calls and fp32: it
- * may be NULL then; at most about 530 bytes per step and value head), free to
+ * may be NULL then; at most about 660 bytes per step and value head), free to
  * use again once the call's work on the stream is done; its contents do not
  * matter.  Calls that may run at the same time, replays of captured graphs
  * among them, need a scratch each.  elem_bytes: 2 for the bf16 call, 4 for

@@ -48,9 +48,11 @@
 // inverse) enter as kParts bf16 parts, and of a product of two of them the
 // part pairs that matter: three parts (all 24 bits, six pairs) where an fp32
 // result leaves the kernel -- the state, or anything of the gradient --, two
-// parts (16 bits, three pairs) where only o does.  Only what reaches nothing
-// but the bf16 output has fewer: S two in Q S0, M one (one for both put the
-// output's error at 1.5 times its own rounding's).
+// parts (16 bits, three pairs) where only o does, and in what reaches nothing
+// but o: S in Q S0, M and r in M r.  16 bits leave the value that is rounded
+// to o within 2^-16 of its terms' size, so that o is the rounding of the exact
+// value but for one step in some 500 (with M in one part its error was 1.4
+// times the rounding's).
 //
 // Bound: the chain of three dependent products per chunk with the loads and
 // conversions between them, not bandwidth: 4100 cycles with 64 columns in two
@@ -80,13 +82,13 @@ struct ChunkScalars {
 constexpr int kScalarBytes = 1024;
 constexpr int kTileBytes = 64 * 128;  // one 64 x 64 bf16 operand
 
-// Scratch of one chunk and head for the chain: the inverse's parts, M where
+// Scratch of one chunk and head for the chain: the inverse's parts, M's two where
 // the mode has it, the scalars; for kReverse also (second buffer) the parts
 // of scale X (I + L')^{-1} and of scale E Q.
 template <int kParts, int kMode>
 struct ChunkImage {
     static constexpr int kM = kParts * kTileBytes;
-    static constexpr int kScalars = kM + (kMode == kFwdOut ? kTileBytes : 0);
+    static constexpr int kScalars = kM + (kMode == kFwdOut ? 2 * kTileBytes : 0);
     static constexpr int kBytes = kScalars + kScalarBytes;
 };
 __host__ __device__ constexpr int second_image_bytes(int ksub) { return 3 * (1 + ksub) * kTileBytes; }
@@ -312,10 +314,7 @@ struct PrepSmem {
         alignas(1024) unsigned char kq[KSUB * 16384];  // per 64 columns: 64 rows of K, 64 of Q
         alignas(16) float t[64 * kChLd];               // then the inverse
     };
-    union {
-        alignas(1024) unsigned char m_tile[kTileBytes];  // M as an operand tile, or
-        alignas(16) float m[kGrad ? 64 * kChLd : 4];     // X
-    };
+    alignas(16) float m[kGrad ? 64 * kChLd : 4];  // X
     alignas(16) float l[64 * kChLd];
     float ghi[kDeltaChunk], glo[kDeltaChunk];  // G_i as two floats
     float e[kDeltaChunk], f[kDeltaChunk], beta[kDeltaChunk];
@@ -323,6 +322,21 @@ struct PrepSmem {
     uint64_t full;
     int dead;
 };
+
+// A 4 x 4 transposition among the four lanes of a quad: word j of lane c becomes
+// word c of lane j.
+__device__ __forceinline__ void quad_transpose(uint32_t (&x)[4], int lane) {
+#pragma unroll
+    for (int s = 1; s <= 2; s *= 2) {
+        const bool up = lane & s;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & s) continue;
+            const uint32_t y = __shfl_xor_sync(0xffffffffu, up ? x[i] : x[i + s], s);
+            (up ? x[i] : x[i + s]) = y;
+        }
+    }
+}
 
 // kGrad: both sweeps' images (kFwdStates and kReverse, three parts), else the
 // forward's.  Grid: chunks * B * HV, heads fastest.
@@ -446,21 +460,41 @@ __global__ void __launch_bounds__(128, kGrad ? (KSUB == 1 ? 4 : 3) : (KSUB == 1 
         }
     };
     put_l(false);
+    const size_t at = blockIdx.x;
+    if constexpr (kGrad) {  // X
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {  // M, or X
-        if (p > 2 * w + 1) continue;
-        const int j = 8 * p + c2;
+        for (int p = 0; p < 8; ++p) {
+            if (p > 2 * w + 1) continue;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int i = i0 + r + 8 * h;
-            if constexpr (kGrad)
-                *reinterpret_cast<float2 *>(&sm.m[i * kChLd + j]) = make_float2(qk[p][2 * h], qk[p][2 * h + 1]);
-            else
-                *reinterpret_cast<uint32_t *>(sm.m_tile + swz128(i, p) + 2 * c2) =
-                    pack_bf16(sm.beta[j] * qk[p][2 * h], sm.beta[j + 1] * qk[p][2 * h + 1]);
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<float2 *>(&sm.m[(i0 + r + 8 * h) * kChLd + 8 * p + c2]) =
+                    make_float2(qk[p][2 * h], qk[p][2 * h + 1]);
+        }
+    } else {
+        // M as two operand tiles, in 16-byte pieces: a quad's four lanes hold
+        // four pieces of every part (two column blocks, two rows), a word each
+        using Img = ChunkImage<kParts, kFwdOut>;
+        unsigned char *img = a.fwd + at * Img::kBytes + Img::kM;
+        const int piece = lane & 3;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            if (m > w) continue;  // warp-uniform
+            uint32_t x[4][2], y[2][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int p = 2 * m + (e >> 1), h = 2 * (e & 1), j = 8 * p + c2;
+                split_bf16<2>(sm.beta[j] * qk[p][h], sm.beta[j + 1] * qk[p][h + 1], x[e]);
+                y[0][e] = x[e][0], y[1][e] = x[e][1];
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                quad_transpose(y[e], lane);
+                *reinterpret_cast<uint4 *>(img + e * kTileBytes +
+                                           swz128(i0 + r + 8 * (piece & 1), 2 * m + (piece >> 1))) =
+                    make_uint4(y[e][0], y[e][1], y[e][2], y[e][3]);
+            }
         }
     }
-    const size_t at = blockIdx.x;
     if constexpr (kGrad) {  // scale E Q
         unsigned char *rev2 = a.rev2 + at * second_image_bytes(KSUB);
 #pragma unroll
@@ -484,13 +518,6 @@ __global__ void __launch_bounds__(128, kGrad ? (KSUB == 1 ? 4 : 3) : (KSUB == 1 
         using Img = ChunkImage<kParts, kFwdOut>;
         unsigned char *img = a.fwd + at * Img::kBytes;
         write_lower<kParts>(sm.t, img, 1.f, tid);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int p = tid + 128 * e, i = p >> 3, c = p & 7;
-            if ((c >> 1) <= (i >> 4))
-                *reinterpret_cast<uint4 *>(img + Img::kM + swz128(i, c)) =
-                    *reinterpret_cast<const uint4 *>(sm.m_tile + swz128(i, c));
-        }
         ChunkScalars *sc = reinterpret_cast<ChunkScalars *>(img + Img::kScalars);
         if (tid < kDeltaChunk) sc->a[tid] = -sm.e[tid], sc->b[tid] = sm.f[tid] * sm.beta[tid];
         if (tid == 0) sc->e_last = sm.e_last;
@@ -792,12 +819,14 @@ __device__ __forceinline__ void delta_chain(const CUtensorMap &map_q, const CUte
                     if (!wait(&sm.m_full, one)) break;
                     tc_fence_after();
 #pragma unroll
-                    for (int p = 0; p < 2; ++p)
+                    for (int w = 1; w >= 0; --w)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tri(k, desc_at(td, Img::kM), [&](uint32_t d, uint64_t t, uint32_t i) {
-                                mma_ts(tm + d, tm + kTmR<kParts> + 32 * p + 8 * k, t, i, p + k > 0);
-                            });
+                        for (int p = 0; p <= w; ++p)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                tri(k, desc_at(td, Img::kM + (w - p) * kTileBytes), [&](uint32_t d, uint64_t t, uint32_t i) {
+                                    mma_ts(tm + d, tm + kTmR<kParts> + 32 * p + 8 * k, t, i, w == 0 || p + k > 0);
+                                });
                     mma_commit(&sm.o_full);
                 }
                 mma_commit(&sm.t_empty[st]);
