@@ -327,7 +327,10 @@ __global__ void __launch_bounds__(256, VW * NI > 8 ? 1 : 2) group_norm_grad_kern
                 if (gated) gv[u][i].get(gt[i]);
             }
             read(u, row + step);
-            const float rstd = norm_center<VW, P, NI>(x, at.lane, a.D, inv_d, a.eps, red);
+            const float spread = norm_center<VW, P, NI>(x, at.lane, a.D, inv_d, a.eps, red);
+            // no token, no spread: with eps = 0 it would be infinite, and its
+            // product with x = 0 would be NaN in the sums over tokens
+            const float rstd = on ? spread : 0.f;
             float m1 = 0.f, m2 = 0.f;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(256, VW * NI > 8 ? 1 : 2) group_norm_grad_kern
                     x[i][e] *= rstd;
                     h[e] = fmaf(x[i][e], wt[i][e], bs[i][e]);
                 }
-                // threads without data have gy = 0: they add nothing
+                // threads without a token have x = gy = 0: they add nothing
                 if (gated) {
                     norm_act_grad<IO, VW>(gt[i], a.act, f, df);
 #pragma unroll
