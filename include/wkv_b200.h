@@ -278,7 +278,10 @@ WKV_API wkv_status diag_scan_bf16(int64_t B, int64_t T, int64_t D,
  *
  * Layout: q, k [B, T, HK, DK]; v, o [B, T, HV, DV]; g, beta [B, T, HV] float;
  * s_in, s_out [B, HV, DK, DV] float, all dense.  HK divides HV (value heads
- * share key heads in order); DK, DV are 1 .. 128.
+ * share key heads in order); DK, DV are at most 128.  Where HV, DK or DV is 0
+ * the call writes zeros, the sums over nothing, to every output that is not
+ * NULL and not empty (o when DK is 0; of the gradients also those of the key
+ * heads when HV or DV is 0).
  * g is the logarithm of the decay: g <= 0, -infinity (forget everything)
  * included.  The recurrence is a contraction for keys of length at most 1 and
  * beta in [0, 1]; other values are computed as they are.  beta = 0 and g = 0

@@ -2,6 +2,7 @@
 // kernel and its launches.  The declarations and their contracts are in
 // include/wkv_b200.h.
 #include <algorithm>
+#include <initializer_list>
 #include <type_traits>
 
 #include "delta_chunk.cuh"
@@ -214,6 +215,37 @@ wkv_status copy_state(float *dst, const float *src, size_t bytes, cudaStream_t s
     return e == cudaSuccess ? WKV_OK : cuda_fail(e, "copy of the state");
 }
 
+// Bytes of a tensor; sizes without a limit (those of calls that compute
+// nothing) end at 2^62, which no allocation holds.
+size_t tensor_bytes(std::initializer_list<int64_t> sizes, size_t elem) {
+    unsigned __int128 n = elem;
+    for (const int64_t s : sizes)
+        if (s == 0) return 0;
+    for (const int64_t s : sizes) n = std::min<unsigned __int128>(n * s, static_cast<unsigned __int128>(1) << 62);
+    return static_cast<size_t>(n);
+}
+
+// A call without value heads, or with heads of no width, has nothing but sums
+// over nothing: those of its outputs that are not empty become zeros.
+template <int N>
+wkv_status zero_outputs(Buf (&bufs)[N], cudaStream_t stream) {
+    bool any = false;
+    for (Buf &b : bufs) {
+        if (b.bytes == 0) b.p = nullptr;  // an empty tensor's pointer may be anything
+        any = any || (b.written && b.p != nullptr);
+    }
+    if (!any) return WKV_OK;
+    int dev = 0;
+    wkv_status st = current_device(&dev);
+    if (st != WKV_OK || (st = check_buffers(bufs, dev)) != WKV_OK) return st;
+    for (const Buf &b : bufs) {
+        if (!b.written || b.p == nullptr) continue;
+        const cudaError_t e = cudaMemsetAsync(const_cast<void *>(b.p), 0, b.bytes, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+    }
+    return WKV_OK;
+}
+
 template <typename IO>
 wkv_status delta_forward(int64_t B, int64_t T, int64_t HK, int64_t HV, int64_t DK, int64_t DV,
                          const void *q, const void *k, const void *v, const float *g,
@@ -222,26 +254,26 @@ wkv_status delta_forward(int64_t B, int64_t T, int64_t HK, int64_t HV, int64_t D
     set_last_error("");
     bool empty = false;
     wkv_status st = check_delta(B, T, HK, HV, DK, DV, &empty);
-    if (st != WKV_OK || empty) return st;
-    const int64_t need = gated_delta_scratch(B, T, HV, DK, DV, sizeof(IO), s_out != nullptr);
-    if (scratch_bytes < need)
+    if (st != WKV_OK) return st;
+    const int64_t need = empty ? 0 : gated_delta_scratch(B, T, HV, DK, DV, sizeof(IO), s_out != nullptr);
+    if (!empty && scratch_bytes < need)
         return fail(WKV_ERR_INVALID_ARG, "scratch has %lld bytes, %lld needed",
                     static_cast<long long>(scratch_bytes), static_cast<long long>(need));
+    const size_t nk = tensor_bytes({B, T, HK, DK}, sizeof(IO)), nv = tensor_bytes({B, T, HV, DV}, sizeof(IO));
+    const size_t ng = tensor_bytes({B, T, HV}, 4), ns = tensor_bytes({B, HV, DK, DV}, 4);
+    const bool none = T == 0 || empty;
+    Buf bufs[] = {{"q", q, nk, sizeof(IO), false, none},
+                  {"k", k, nk, sizeof(IO), false, none},
+                  {"v", v, nv, sizeof(IO), false, none},
+                  {"g", g, ng, 4, false, none},
+                  {"beta", beta, ng, 4, false, none},
+                  {"o", o, nv, sizeof(IO), true, none},
+                  {"s_in", s_in, ns, 4, false, true},
+                  {"s_out", s_out, ns, 4, true, true},
+                  {"scratch", need > 0 ? scratch : nullptr, static_cast<size_t>(need), 16, true, need == 0}};
+    if (empty) return zero_outputs(bufs, stream);
     int dev = 0;
     if ((st = current_device(&dev)) != WKV_OK) return st;
-    const size_t tokens = static_cast<size_t>(B) * T;
-    const size_t nk = tokens * HK * DK * sizeof(IO), nv = tokens * HV * DV * sizeof(IO);
-    const size_t ng = tokens * HV * 4, ns = static_cast<size_t>(B) * HV * DK * DV * 4;
-    const bool none = T == 0;
-    const Buf bufs[] = {{"q", q, nk, sizeof(IO), false, none},
-                        {"k", k, nk, sizeof(IO), false, none},
-                        {"v", v, nv, sizeof(IO), false, none},
-                        {"g", g, ng, 4, false, none},
-                        {"beta", beta, ng, 4, false, none},
-                        {"o", o, nv, sizeof(IO), true, none},
-                        {"s_in", s_in, ns, 4, false, true},
-                        {"s_out", s_out, ns, 4, true, true},
-                        {"scratch", need > 0 ? scratch : nullptr, static_cast<size_t>(need), 16, true, need == 0}};
     if ((st = check_buffers(bufs, dev, 6, 7)) != WKV_OK) return st;
     if (none) return copy_state(s_out, s_in, ns, stream);
     DeltaFwdArgs<IO> a{};
@@ -308,32 +340,32 @@ wkv_status delta_backward(int64_t B, int64_t T, int64_t HK, int64_t HV, int64_t 
     set_last_error("");
     bool empty = false;
     wkv_status st = check_delta(B, T, HK, HV, DK, DV, &empty);
-    if (st != WKV_OK || empty) return st;
-    const int64_t need = gated_delta_backward_scratch(B, T, HV, DK, DV, sizeof(IO));
-    if (scratch_bytes < need)
+    if (st != WKV_OK) return st;
+    const int64_t need = empty ? 0 : gated_delta_backward_scratch(B, T, HV, DK, DV, sizeof(IO));
+    if (!empty && scratch_bytes < need)
         return fail(WKV_ERR_INVALID_ARG, "scratch has %lld bytes, %lld needed",
                     static_cast<long long>(scratch_bytes), static_cast<long long>(need));
+    const size_t nk = tensor_bytes({B, T, HK, DK}, sizeof(IO)), nv = tensor_bytes({B, T, HV, DV}, sizeof(IO));
+    const size_t ng = tensor_bytes({B, T, HV}, 4), ns = tensor_bytes({B, HV, DK, DV}, 4);
+    const bool none = T == 0 || empty;
+    Buf bufs[] = {{"q", q, nk, sizeof(IO), false, none},
+                  {"k", k, nk, sizeof(IO), false, none},
+                  {"v", v, nv, sizeof(IO), false, none},
+                  {"g", g, ng, 4, false, none},
+                  {"beta", beta, ng, 4, false, none},
+                  {"go", go, nv, sizeof(IO), false, none},
+                  {"s_in", s_in, ns, 4, false, true},
+                  {"gs_out", gs_out, ns, 4, false, true},
+                  {"gq", gq, nk, sizeof(IO), true, none},
+                  {"gk", gk, nk, sizeof(IO), true, none},
+                  {"gv", gv, nv, sizeof(IO), true, none},
+                  {"gg", gg, ng, 4, true, none},
+                  {"gbeta", gbeta, ng, 4, true, none},
+                  {"gs_in", gs_in, ns, 4, true, true},
+                  {"scratch", need > 0 ? scratch : nullptr, static_cast<size_t>(need), 16, true, need == 0}};
+    if (empty) return zero_outputs(bufs, stream);
     int dev = 0;
     if ((st = current_device(&dev)) != WKV_OK) return st;
-    const size_t tokens = static_cast<size_t>(B) * T;
-    const size_t nk = tokens * HK * DK * sizeof(IO), nv = tokens * HV * DV * sizeof(IO);
-    const size_t ng = tokens * HV * 4, ns = static_cast<size_t>(B) * HV * DK * DV * 4;
-    const bool none = T == 0;
-    const Buf bufs[] = {{"q", q, nk, sizeof(IO), false, none},
-                        {"k", k, nk, sizeof(IO), false, none},
-                        {"v", v, nv, sizeof(IO), false, none},
-                        {"g", g, ng, 4, false, none},
-                        {"beta", beta, ng, 4, false, none},
-                        {"go", go, nv, sizeof(IO), false, none},
-                        {"s_in", s_in, ns, 4, false, true},
-                        {"gs_out", gs_out, ns, 4, false, true},
-                        {"gq", gq, nk, sizeof(IO), true, none},
-                        {"gk", gk, nk, sizeof(IO), true, none},
-                        {"gv", gv, nv, sizeof(IO), true, none},
-                        {"gg", gg, ng, 4, true, none},
-                        {"gbeta", gbeta, ng, 4, true, none},
-                        {"gs_in", gs_in, ns, 4, true, true},
-                        {"scratch", scratch, static_cast<size_t>(need), 16, true, none}};
     if ((st = check_buffers(bufs, dev)) != WKV_OK) return st;
     if (none) return copy_state(gs_in, gs_out, ns, stream);
     const Scratch sc(B, T, HV, DK, DV, sizeof(IO));

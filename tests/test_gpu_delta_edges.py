@@ -1,5 +1,5 @@
 """The gated delta rule where its answers are easily a little or wholly off:
-roundings of bf16 outputs.
+roundings of bf16 outputs, sizes of 0.
 
 The oracle is the float64 step-by-step one; it is fed the rounded inputs.
 """
@@ -65,3 +65,20 @@ def test_bf16_outputs_are_rounded_once(m, shape, with_state):
     rms = np.sqrt((want ** 2).mean())
     over = (np.abs(got - want) - half) / rms
     assert over.max() <= 2.0 ** -12, f"{over.max():.2e} of the rms beyond the rounding, {np.mean(over > 2.0 ** -12):.1%}"
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 5, 1, 2, 0, 8), (2, 5, 1, 2, 8, 0), (2, 70, 2, 0, 8, 16), (1, 3, 2, 0, 0, 0)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_sums_over_nothing_are_zero(m, shape, dtype):
+    """Key or value heads without width, or no value heads: what is not empty
+    of the outputs is a sum over nothing, not what its memory held."""
+    x = draw(*shape, dtype=dtype, seed=3)
+    nan = {n: torch.full_like(x[n], float("nan")) for n in ("q", "k", "v", "g", "beta")}
+    o = nan["v"].clone()
+    m.gated_delta(*(x[n] for n in INPUTS), s_in=x["s_in"], o=o, s_out=torch.empty_like(x["s_in"]))
+    assert o.shape == x["v"].shape and (o == 0).all()
+    del nan     # its blocks, full of NaN, are what the next outputs are handed
+    grads = m.gated_delta_backward(*(x[n] for n in INPUTS), x["go"], s_in=x["s_in"], gs_out=x["gs_out"])
+    for name, gr in zip(INPUTS + ("s_in",), grads):
+        assert gr.shape == x[name].shape and (gr == 0).all(), name
