@@ -16,6 +16,12 @@ raises if the library has not been built.
     y = wkv_forward_host(w, u, k, v)       # the same on CPU tensors, copies overlapped
     o = gated_delta(q, k, v, g, beta, s_in=s, s_out=s)   # matrix state per head, in place
     y = group_norm(o.reshape(B, T, -1), H, weight, bias, gate=z, act="silu")
+
+A call with ``stream=s`` is a call under ``torch.cuda.stream(s)``: what it
+returns and its scratch are allocated on s, as torch's own results there would
+be.  The caller orders s after the work that makes the inputs, and what reads
+the results elsewhere after s (and says ``record_stream`` before dropping a
+result that another stream still reads, or an input that s does).
 """
 from __future__ import annotations
 
@@ -103,6 +109,25 @@ def _stream_handle(stream):
     return stream.cuda_stream
 
 
+def _empty(shape, dtype, like, stream):
+    """Device memory for one call on `stream`: from torch's caching allocator,
+    allocated on that stream, so that it is neither handed out while work of
+    another stream uses it nor again before the call's work is done."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _empty_like(t, stream):
+    import torch
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
+
+
 def _need(t, name, dtype, ndim):
     import torch
     if not isinstance(t, torch.Tensor):
@@ -129,7 +154,7 @@ def _wkv(fn_name, io_dtype, w, u, k, v, y, stream):
     if w.shape[0] != C or u.shape[0] != C:
         raise ValueError("w and u must be [C]")
     if y is None:
-        y = torch.empty_like(k)
+        y = _empty_like(k, stream)
     else:
         _need(y, "y", io_dtype, 3)
         if y.shape != k.shape:
@@ -161,7 +186,7 @@ def _wkv_state(fn_name, io_dtype, w, u, k, v, s_in, y, s_out, stream):
             if tuple(t.shape) != (B, 3, C):
                 raise ValueError(f"{name} must be [B, 3, C] = {(B, 3, C)}")
     if s_out is None:
-        s_out = torch.empty((B, 3, C), dtype=torch.float32, device=k.device)
+        s_out = _empty((B, 3, C), torch.float32, k, stream)
     _need(v, "v", io_dtype, 3)
     _need(w, "w", torch.float32, 1)
     _need(u, "u", torch.float32, 1)
@@ -170,7 +195,7 @@ def _wkv_state(fn_name, io_dtype, w, u, k, v, s_in, y, s_out, stream):
     if w.shape[0] != C or u.shape[0] != C:
         raise ValueError("w and u must be [C]")
     if y is None:
-        y = torch.empty_like(k)
+        y = _empty_like(k, stream)
     else:
         _need(y, "y", io_dtype, 3)
         if y.shape != k.shape:
@@ -222,7 +247,7 @@ def wkv_forward_gated(w, u, k, v, r, y=None, s_in=None, s_out=None, stream=None)
             if tuple(t.shape) != (B, 3, C):
                 raise ValueError(f"{name} must be [B, 3, C] = {(B, 3, C)}")
     if y is None:
-        y = torch.empty_like(k)
+        y = _empty_like(k, stream)
     else:
         _need(y, "y", io, 3)
         if y.shape != k.shape:
@@ -257,7 +282,7 @@ def token_shift(x, mu, x_prev=None, out=None, x_last=None, stream=None):
             if tuple(t.shape) != (B, C):
                 raise ValueError(f"{name} must be [B, C] = {(B, C)}")
     if out is None:
-        out = torch.empty((n_mix, B, T, C), dtype=io, device=x.device)
+        out = _empty((n_mix, B, T, C), io, x, stream)
     else:
         _need(out, "out", io, 4)
         if tuple(out.shape) != (n_mix, B, T, C):
@@ -296,7 +321,7 @@ def diag_scan(a, b, h0=None, h=None, stream=None):
         if tuple(h0.shape) != (B, D):
             raise ValueError("h0 must be [B, D]")
     if h is None:
-        h = torch.empty_like(a)
+        h = _empty_like(a, stream)
     else:
         _need(h, "h", io, 3)
         if h.shape != a.shape:
@@ -321,8 +346,8 @@ def wkv_backward(w, u, k, v, gy, stream=None):
     B, T, C = k.shape
     if w.shape[0] != C or u.shape[0] != C:
         raise ValueError("w and u must be [C]")
-    gk, gv = torch.empty_like(k), torch.empty_like(k)
-    gw, gu = torch.empty_like(w), torch.empty_like(u)
+    gk, gv = _empty_like(k, stream), _empty_like(k, stream)
+    gw, gu = _empty_like(w, stream), _empty_like(u, stream)
     _check(lib.wkv_backward(B, T, C, w.data_ptr(), u.data_ptr(), k.data_ptr(), v.data_ptr(),
                             gy.data_ptr(), gk.data_ptr(), gv.data_ptr(), gw.data_ptr(),
                             gu.data_ptr(), _stream_handle(stream)), "wkv_backward")
@@ -353,7 +378,7 @@ def lru_scan(nu_log, theta_log, u, gamma=None, x0=None, x=None, stream=None):
         if tuple(x0r.shape) != (B, D, 2):
             raise ValueError("x0 must be [B, D] complex")
     if x is None:
-        x = torch.empty_like(u)
+        x = _empty_like(u, stream)
     xr = torch.view_as_real(x) if x.dtype == torch.complex64 else x
     _need(xr, "x", torch.float32, 4)
     if xr.shape != ur.shape:
@@ -387,14 +412,8 @@ def _tensor(t, name, dtype, shape):
 
 
 def _scratch(n, like, stream):
-    """n bytes of device memory for one call on `stream`: from torch's caching
-    allocator, allocated on that stream, so it is not handed out again before
-    the call's work there is done."""
     import torch
-    if stream is None:
-        return torch.empty(n, dtype=torch.uint8, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(n, dtype=torch.uint8, device=like.device)
+    return _empty(n, torch.uint8, like, stream)
 
 
 def _delta_scale(scale, DK):
@@ -435,7 +454,7 @@ def gated_delta(q, k, v, g, beta, scale=None, s_in=None, o=None, s_out=None, str
         if t is not None:
             _tensor(t, name, torch.float32, (B, HV, DK, DV))
     if o is None:
-        o = torch.empty_like(v)
+        o = torch.empty_like(v) if stream is None else _empty_like(v, stream)
     else:
         _tensor(o, "o", io, v.shape)
     fn = "gated_delta" if io == torch.float32 else "gated_delta_bf16"
@@ -460,9 +479,9 @@ def gated_delta_backward(q, k, v, g, beta, go, scale=None, s_in=None, gs_out=Non
     for t, name in ((s_in, "s_in"), (gs_out, "gs_out")):
         if t is not None:
             _tensor(t, name, torch.float32, (B, HV, DK, DV))
-    gq, gk, gv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    gg, gbeta = torch.empty_like(g), torch.empty_like(beta)
-    gs_in = None if s_in is None else torch.empty_like(s_in)
+    gq, gk, gv = _empty_like(q, stream), _empty_like(k, stream), _empty_like(v, stream)
+    gg, gbeta = _empty_like(g, stream), _empty_like(beta, stream)
+    gs_in = None if s_in is None else _empty_like(s_in, stream)
     n = lib.gated_delta_backward_scratch(B, T, HV, DK, DV, q.element_size())
     scratch = _scratch(n, q, stream)
     fn = "gated_delta_backward" if io == torch.float32 else "gated_delta_backward_bf16"
@@ -507,7 +526,7 @@ def group_norm(x, groups, weight=None, bias=None, gate=None, act="none", eps=1e-
     import torch
     io, N, C, code = _norm_sizes(x, groups, weight, bias, gate, act)
     if y is None:
-        y = torch.empty_like(x)
+        y = torch.empty_like(x) if stream is None else _empty_like(x, stream)
     else:
         _tensor(y, "y", io, x.shape)
     fn = "group_norm" if io == torch.float32 else "group_norm_bf16"
@@ -523,10 +542,10 @@ def group_norm_backward(x, gy, groups, weight=None, bias=None, gate=None, act="n
     import torch
     io, N, C, code = _norm_sizes(x, groups, weight, bias, gate, act)
     _tensor(gy, "gy", io, x.shape)
-    gx = torch.empty_like(x)
-    gweight = None if weight is None else torch.empty_like(weight)
-    gbias = None if bias is None else torch.empty_like(bias)
-    ggate = None if gate is None else torch.empty_like(gate)
+    gx = _empty_like(x, stream)
+    gweight = None if weight is None else _empty_like(weight, stream)
+    gbias = None if bias is None else _empty_like(bias, stream)
+    ggate = None if gate is None else _empty_like(gate, stream)
     n = lib.group_norm_backward_scratch(N, C)
     scratch = _scratch(n, x, stream)
     fn = "group_norm_backward" if io == torch.float32 else "group_norm_backward_bf16"
