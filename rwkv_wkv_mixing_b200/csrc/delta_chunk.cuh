@@ -670,7 +670,7 @@ __device__ __forceinline__ void delta_chain(const CUtensorMap &map_q, const CUte
             for (int c = 0; c < chunks; ++c) {
                 const int st = c & 1, ck = chunk_at(c), t0 = ck * kDeltaChunk;
                 const uint32_t free = ((c >> 1) & 1) ^ 1;
-                if (!mbar_wait(&sm.kq_empty[st], free, dead)) break;
+                if (!mbar_wait_one(&sm.kq_empty[st], free, dead)) break;
                 mbar_arrive_expect_tx(&sm.kq_full[st], KSUB * Smem::kBlock);
 #pragma unroll
                 for (int s = 0; s < KSUB; ++s) {
@@ -679,17 +679,17 @@ __device__ __forceinline__ void delta_chain(const CUtensorMap &map_q, const CUte
                     if constexpr (kOut) tma_load_4d(p + 8192, &map_q, &sm.kq_full[st], 64 * s, hk, t0, b);
                 }
                 ++nk;
-                if (!mbar_wait(&sm.t_empty[st], free, dead)) break;
+                if (!mbar_wait_one(&sm.t_empty[st], free, dead)) break;
                 mbar_arrive_expect_tx(&sm.t_full[st], Img::kBytes);
                 bulk_load(sm.img[st], a.img + (ck * heads + bh) * Img::kBytes, Img::kBytes, &sm.t_full[st]);
                 ++nt;
-                if (!mbar_wait(&sm.v_empty[st], free, dead)) break;
+                if (!mbar_wait_one(&sm.v_empty[st], free, dead)) break;
                 mbar_arrive_expect_tx(&sm.v_full[st], 8192 * vblocks);
                 for (int s = 0; s < vblocks; ++s)
                     tma_load_4d(sm.v[st] + 8192 * s, &map_v, &sm.v_full[st], 64 * s, hv, t0, b);
                 ++nv;
                 if constexpr (kRev) {
-                    if (!mbar_wait(&sm.z_empty, (c & 1) ^ 1, dead)) break;
+                    if (!mbar_wait_one(&sm.z_empty, (c & 1) ^ 1, dead)) break;
                     mbar_arrive_expect_tx(&sm.z_full, Smem::kImage2);
                     bulk_load(sm.img2, a.img2 + (ck * heads + bh) * Smem::kImage2, Smem::kImage2, &sm.z_full);
                     ++nz;
@@ -704,9 +704,7 @@ __device__ __forceinline__ void delta_chain(const CUtensorMap &map_q, const CUte
         } else if (warp == kLoadWarp + 1) {
             // ---- tcgen05.mma ----
             // (the whole warp: see mma_ts)
-            const auto wait = [&](uint64_t *bar, uint32_t parity) {
-                return __all_sync(0xffffffffu, mbar_wait(bar, parity, dead));
-            };
+            const auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, dead); };
             // columns beyond DK are zeros in K's tile and in S: full widths
             constexpr uint32_t i_64 = mma_idesc(64, false);
             constexpr uint32_t i_ds = mma_idesc(64 * KSUB, true);

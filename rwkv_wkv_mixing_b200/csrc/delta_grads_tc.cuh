@@ -208,9 +208,7 @@ __global__ void __launch_bounds__(kTcGradThreads, 1)
                 }
             }
         };
-        const auto wait = [&](uint64_t *bar, int n) {
-            return __all_sync(0xffffffffu, mbar_wait(bar, n & 1, dead));
-        };
+        const auto wait = [&](uint64_t *bar, int n) { return mbar_wait(bar, n & 1, dead); };
         bool on = wait(&sm.tile, 0);
         int q = 0;
         for (int gh = 0; on && gh < z.group; ++gh) {
@@ -255,7 +253,7 @@ __global__ void __launch_bounds__(kTcGradThreads, 1)
         if (lane == 0) {
             for (; q < min(all, 2); ++q) fetch(q);
             for (; q < all; ++q) {
-                if (!mbar_wait(&sm.ready[q & 1], ((q - 2) >> 1) & 1, dead)) break;
+                if (!mbar_wait_one(&sm.ready[q & 1], ((q - 2) >> 1) & 1, dead)) break;
                 fetch(q);
             }
             for (int d = max(0, q - 2); d < q; ++d) mbar_drain(&sm.full[d & 1], (d >> 1) & 1);

@@ -17,16 +17,30 @@ namespace wkvb {
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 
 // Waits for the barrier's phase.  False once the wait gave up or another
-// thread's did (`dead`, in shared memory, tells the block).
+// warp's did (`dead`, in shared memory, tells the block).  A whole warp calls it
+// and gets one answer: with a lane's own, a wait that gives up could part the
+// warp before an instruction that needs all of it.
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *dead) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const unsigned long long start = global_timer_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if ((i & 7) == 0 &&
+            __any_sync(0xffffffffu, *dead != 0 || global_timer_ns() - start > kWaitLimitNs))
+            break;
+    }
+    *dead = 1;
+    return false;
+}
+
+// The same for one thread.
+__device__ __forceinline__ bool mbar_wait_one(uint64_t *bar, uint32_t parity, volatile int *dead) {
     const unsigned long long start = global_timer_ns();
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 63) == 0) {
-            if (*dead) return false;
-            if (global_timer_ns() - start > kWaitLimitNs) break;
-        }
+        if ((i & 7) == 0 &&
+            (*dead != 0 || global_timer_ns() - start > kWaitLimitNs))
+            break;
     }
     *dead = 1;
     return false;
