@@ -64,7 +64,8 @@
  *           inputs) are documented, not checked: NaN propagates.
  *           A device-side wait that gives up (see wkv_device_status) writes
  *           NaN outputs for the affected tile and raises WKV_ERR_TIMEOUT
- *           instead of hanging.
+ *           instead of hanging (where a declaration below does not say
+ *           otherwise).
  */
 #ifndef WKV_B200_H
 #define WKV_B200_H
@@ -298,7 +299,10 @@ WKV_API wkv_status diag_scan_bf16(int64_t B, int64_t T, int64_t D,
  * use again once the call's work on the stream is done; its contents do not
  * matter.  Calls that may run at the same time, replays of captured graphs
  * among them, need a scratch each.  elem_bytes: 2 for the bf16 call, 4 for
- * fp32; with_state: whether s_out is given. */
+ * fp32; with_state: whether s_out is given.
+ * A device-side wait that gives up (of these calls and their gradients) leaves
+ * NaN in every output that depends on it; wkv_device_status does not report
+ * it, since they use no workspace of the library. */
 WKV_API int64_t gated_delta_scratch(int64_t B, int64_t T, int64_t HV, int64_t DK, int64_t DV,
                                     int elem_bytes, int with_state);
 WKV_API wkv_status gated_delta(int64_t B, int64_t T, int64_t HK, int64_t HV, int64_t DK,
@@ -347,6 +351,15 @@ WKV_API wkv_status gated_delta_backward_bf16(int64_t B, int64_t T, int64_t HK, i
                                              wkv_bf16_t *gv, float *gg, float *gbeta,
                                              float *gs_in, void *scratch, int64_t scratch_bytes,
                                              cudaStream_t stream);
+
+/* Test hook for the bounded waits of the gated delta rule's bf16 kernels over
+ * chunks of 64 steps, process-wide, for later launches.  kernel 1 (preparation
+ * of the chunks), 2 (the chain of the states) or 3 (gradients within a chunk)
+ * does not make chunk `chunk`'s copies (2: nor any after it in its direction),
+ * so the waits for them run out, after 2 seconds.  The outcome is NaN in the
+ * outputs that depend on the chunk; the context stays usable.  (0, 0) turns it
+ * off.  WKV_ERR_INVALID_ARG for values out of range. */
+WKV_API wkv_status gated_delta_set_fault_injection(int kernel, int chunk);
 
 /* Group norm with an activation, channels last: the normalisation and gate
  * between a recurrence over heads and the output projection.  Each of N tokens

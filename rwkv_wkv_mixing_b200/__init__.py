@@ -69,6 +69,7 @@ _SIGS = {
     "gated_delta_backward_scratch": ([_i64] * 5 + [_i32], _i64),
     "gated_delta_backward": ([_i64] * 6 + [_p] * 5 + [_f32] + [_p] * 10 + [_i64, _p], _i32),
     "gated_delta_backward_bf16": ([_i64] * 6 + [_p] * 5 + [_f32] + [_p] * 10 + [_i64, _p], _i32),
+    "gated_delta_set_fault_injection": ([_i32] * 2, _i32),
     "group_norm": ([_i64] * 3 + [_p] * 4 + [_i32, _f32, _p, _p], _i32),
     "group_norm_bf16": ([_i64] * 3 + [_p] * 4 + [_i32, _f32, _p, _p], _i32),
     "group_norm_backward_scratch": ([_i64] * 2, _i64),
@@ -653,6 +654,13 @@ def wkv_get_tile_steps() -> int:
 def wkv_tile_steps_for(B: int, T: int, C: int, elem_bytes: int = 4) -> int:
     """The tile length a call of this shape uses under the current knob."""
     return int(lib.wkv_tile_steps_for(B, T, C, elem_bytes))
+
+
+def gated_delta_set_fault_injection(kernel: int = 0, chunk: int = 0):
+    """Test hook: kernel 1, 2 or 3 of the gated delta rule's bf16 calls does not
+    make one 64-step chunk's copies, and the waits for them run out.  No
+    arguments: off."""
+    _check(lib.gated_delta_set_fault_injection(kernel, chunk), "gated_delta_set_fault_injection")
 
 
 def wkv_set_fault_injection(skip_tile: int = -1, spin_limit: int = 0):

@@ -2,6 +2,7 @@
 // kernel and its launches.  The declarations and their contracts are in
 // include/wkv_b200.h.
 #include <algorithm>
+#include <atomic>
 #include <initializer_list>
 #include <type_traits>
 
@@ -16,6 +17,11 @@ using namespace wkvb;
 namespace {
 
 using bf16 = __nv_bfloat16;
+
+// ---- test hook (see gated_delta_set_fault_injection) ----
+std::atomic<int> g_fault_kernel{0}, g_fault_chunk{0};
+
+int silent_chunk(int kernel) { return g_fault_kernel.load() == kernel ? g_fault_chunk.load() : -1; }
 
 wkv_status check_delta(int64_t B, int64_t T, int64_t HK, int64_t HV, int64_t DK, int64_t DV,
                        bool *empty) {
@@ -285,8 +291,8 @@ wkv_status delta_forward(int64_t B, int64_t T, int64_t HK, int64_t HV, int64_t D
         CUtensorMap m[3];
         if (need > 0 && chunked_fits(a.z, q, k, v) && make_map(&m[0], q, a.z, a.z.HK, a.z.DK) &&
             make_map(&m[1], k, a.z, a.z.HK, a.z.DK) && make_map(&m[2], v, a.z, a.z.HV, a.z.DV)) {
-            const DeltaPrepArgs p{g, beta, static_cast<unsigned char *>(scratch), nullptr, nullptr, scale, a.z};
-            const DeltaChainArgs c{p.fwd, nullptr, s_in, a.o, s_out, nullptr, nullptr, scale, a.z};
+            const DeltaPrepArgs p{g, beta, static_cast<unsigned char *>(scratch), nullptr, nullptr, scale, a.z, silent_chunk(1)};
+            const DeltaChainArgs c{p.fwd, nullptr, s_in, a.o, s_out, nullptr, nullptr, scale, a.z, silent_chunk(2)};
             const bool small = a.z.DK <= 64;
             if (s_out == nullptr)
                 return small ? launch_forward<1, 2>(p, c, m, dev, stream) : launch_forward<2, 2>(p, c, m, dev, stream);
@@ -392,11 +398,11 @@ wkv_status delta_backward(int64_t B, int64_t T, int64_t HK, int64_t HV, int64_t 
             make_map(&m[2], v, z, z.HV, z.DV) && make_map(&m[3], go, z, z.HV, z.DV) &&
             make_map(&m[4], gv, z, z.HV, z.DV)) {
             unsigned char *img = static_cast<unsigned char *>(scratch);
-            const DeltaPrepArgs p{g, beta, img + sc.fwd, img + sc.rev, img + sc.rev2, scale, z};
-            const DeltaChainArgs fa{p.fwd, nullptr, s_in, nullptr, nullptr, r, starts, scale, z};
-            const DeltaChainArgs ra{p.rev, p.rev2, gs_out, nullptr, gs_in, du, ends, scale, z};
+            const DeltaPrepArgs p{g, beta, img + sc.fwd, img + sc.rev, img + sc.rev2, scale, z, silent_chunk(1)};
+            const DeltaChainArgs fa{p.fwd, nullptr, s_in, nullptr, nullptr, r, starts, scale, z, silent_chunk(2)};
+            const DeltaChainArgs ra{p.rev, p.rev2, gs_out, nullptr, gs_in, du, ends, scale, z, silent_chunk(2)};
             const DeltaTcGradArgs tg{g, beta, r, du, starts, ends, static_cast<IO *>(gq), static_cast<IO *>(gk),
-                                     gg, gbeta, scale, z};
+                                     static_cast<IO *>(gv), gg, gbeta, scale, z, silent_chunk(3)};
             return z.DK <= 64 ? launch_gradient<1>(p, fa, ra, tg, m, dev, stream)
                               : launch_gradient<2>(p, fa, ra, tg, m, dev, stream);
         }
@@ -443,6 +449,15 @@ wkv_status gated_delta_bf16(int64_t B, int64_t T, int64_t HK, int64_t HV, int64_
                             int64_t scratch_bytes, cudaStream_t stream) {
     return delta_forward<bf16>(B, T, HK, HV, DK, DV, q, k, v, g, beta, scale, o, s_in, s_out,
                                scratch, scratch_bytes, stream);
+}
+
+wkv_status gated_delta_set_fault_injection(int kernel, int chunk) {
+    set_last_error("");
+    if (kernel < 0 || kernel > 3 || chunk < 0)
+        return fail(WKV_ERR_INVALID_ARG, "kernel must be 0 .. 3, chunk >= 0");
+    g_fault_kernel.store(kernel);
+    g_fault_chunk.store(chunk);
+    return WKV_OK;
 }
 
 int64_t gated_delta_scratch(int64_t B, int64_t T, int64_t HV, int64_t DK, int64_t DV, int elem_bytes,

@@ -111,6 +111,7 @@ struct DeltaPrepArgs {
     unsigned char *fwd, *rev, *rev2;  // images [chunks][B * HV]
     float scale;
     DeltaSizes z;
+    int silent;  // for tests of the bounded waits: the chunk whose copies are not made, or -1
 };
 
 struct DeltaChainArgs {
@@ -122,6 +123,7 @@ struct DeltaChainArgs {
     float *states;                    // S0 or D1, of DK rows: as sweep_at() says
     float scale;
     DeltaSizes z;
+    int silent;  // for tests of the bounded waits: the chunk whose copies are not made, or -1
 };
 
 constexpr int kChLd = 68;  // floats per row of the 64 x 64 fp32 work matrices
@@ -354,15 +356,18 @@ __global__ void __launch_bounds__(128, kGrad ? (KSUB == 1 ? 4 : 3) : (KSUB == 1 
     const unsigned heads = static_cast<unsigned>(z.B) * z.HV, bh = blockIdx.x % heads;
     const int b = static_cast<int>(bh / z.HV), hv = static_cast<int>(bh % z.HV), hk = hv / z.group;
     const int t0 = static_cast<int>(blockIdx.x / heads) * kDeltaChunk;
+    const bool silent = t0 / kDeltaChunk == a.silent;
     if (tid == 0) {
         sm.dead = 0;
         mbar_init(&sm.full, 1);
         fence_mbar_init();
-        mbar_arrive_expect_tx(&sm.full, KSUB * 16384);
+        if (!silent) {
+            mbar_arrive_expect_tx(&sm.full, KSUB * 16384);
 #pragma unroll
-        for (int s = 0; s < KSUB; ++s) {
-            tma_load_4d(sm.kq + s * 16384, &map_k, &sm.full, 64 * s, hk, t0, b);
-            tma_load_4d(sm.kq + s * 16384 + 8192, &map_q, &sm.full, 64 * s, hk, t0, b);
+            for (int s = 0; s < KSUB; ++s) {
+                tma_load_4d(sm.kq + s * 16384, &map_k, &sm.full, 64 * s, hk, t0, b);
+                tma_load_4d(sm.kq + s * 16384 + 8192, &map_q, &sm.full, 64 * s, hk, t0, b);
+            }
         }
     }
     __syncthreads();
@@ -382,7 +387,9 @@ __global__ void __launch_bounds__(128, kGrad ? (KSUB == 1 ? 4 : 3) : (KSUB == 1 
         if (lane == 0) sm.e_last = expf(static_cast<float>(last));
     }
     // a copy that never lands leaves NaN behind, not old tiles' values
-    const float poison = mbar_wait(&sm.full, 0, &sm.dead) ? 0.f : __int_as_float(0x7FC00000);
+    const bool landed = mbar_wait(&sm.full, 0, &sm.dead);
+    if (!landed && !silent && tid == 0) mbar_drain(&sm.full, 0);
+    const float poison = landed ? 0.f : __int_as_float(0x7FC00000);
 
     // K K^T and Q K^T: this warp's 16 rows, columns up to the diagonal
     const int i0 = 16 * w, r = lane >> 2, c2 = 2 * (lane & 3);
@@ -441,7 +448,7 @@ __global__ void __launch_bounds__(128, kGrad ? (KSUB == 1 ? 4 : 3) : (KSUB == 1 
                     if (p < 2 * w) d = er[h] * fc[p < 6 ? p : 0][e];
                     else d = i >= j ? expf((sm.ghi[i] - sm.ghi[j]) + (sm.glo[i] - sm.glo[j])) : 0.f;
                     kk[p][2 * h + e] = i > j ? d * kk[p][2 * h + e] + poison : 0.f;
-                    qk[p][2 * h + e] = i >= j ? d * qk[p][2 * h + e] : 0.f;
+                    qk[p][2 * h + e] = i >= j ? d * qk[p][2 * h + e] + poison : 0.f;
                 }
         }
     }
@@ -502,7 +509,7 @@ __global__ void __launch_bounds__(128, kGrad ? (KSUB == 1 ? 4 : 3) : (KSUB == 1 
             const int p = tid + 128 * e, s = p >> 9, i = (p >> 3) & 63, c = p & 7;
             const uint4 v = *reinterpret_cast<const uint4 *>(sm.kq + s * 16384 + 8192 + swz128(i, c));
             const uint32_t vv[4] = {v.x, v.y, v.z, v.w};
-            const float f = a.scale * sm.e[i];
+            const float f = a.scale * sm.e[i] + poison;
             uint32_t y[4][3];
 #pragma unroll
             for (int q = 0; q < 4; ++q) split_bf16<3>(f * bf16_low(vv[q]), f * bf16_high(vv[q]), y[q]);
@@ -670,6 +677,7 @@ __device__ __forceinline__ void delta_chain(const CUtensorMap &map_q, const CUte
             for (int c = 0; c < chunks; ++c) {
                 const int st = c & 1, ck = chunk_at(c), t0 = ck * kDeltaChunk;
                 const uint32_t free = ((c >> 1) & 1) ^ 1;
+                if (ck == a.silent) break;
                 if (!mbar_wait_one(&sm.kq_empty[st], free, dead)) break;
                 mbar_arrive_expect_tx(&sm.kq_full[st], KSUB * Smem::kBlock);
 #pragma unroll

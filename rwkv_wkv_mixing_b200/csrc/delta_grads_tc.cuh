@@ -38,10 +38,11 @@ namespace wkvb {
 struct DeltaTcGradArgs {
     const float *g, *beta;
     const float *r, *du, *starts, *ends;  // as the sweeps left them (sweep_at)
-    __nv_bfloat16 *gq, *gk;
+    __nv_bfloat16 *gq, *gk, *gv;          // gv by its tensor map
     float *gg, *gbeta;
     float scale;
     DeltaSizes z;
+    int silent;  // as in DeltaPrepArgs
 };
 
 constexpr int kTcWorkers = 512, kTcGradThreads = kTcWorkers + 64;
@@ -81,7 +82,7 @@ struct TcGradSmem {
     float sums[8][kDeltaChunk];
     float part[kTcWorkers / 32];
     float e_last;
-    uint64_t tile, full[2], ready[2], done[2], ready_xy, done_xy;
+    uint64_t tile, full[2], ready[2], done[2], ready_xy, done_xy, drain;
     uint32_t tmem;
     int dead;
 };
@@ -135,7 +136,8 @@ __global__ void __launch_bounds__(kTcGradThreads, 1)
 
     if (tid == 0) {
         sm.dead = 0;
-        for (uint64_t *p : {&sm.tile, &sm.full[0], &sm.full[1], &sm.done[0], &sm.done[1], &sm.done_xy}) mbar_init(p, 1);
+        for (uint64_t *p : {&sm.tile, &sm.full[0], &sm.full[1], &sm.done[0], &sm.done[1], &sm.done_xy, &sm.drain})
+            mbar_init(p, 1);
         for (uint64_t *p : {&sm.ready[0], &sm.ready[1], &sm.ready_xy}) mbar_init(p, kTcWorkers);
         fence_mbar_init();
         mbar_arrive_expect_tx(&sm.tile, KSUB * 16384);
@@ -241,14 +243,12 @@ __global__ void __launch_bounds__(kTcGradThreads, 1)
             mma_commit(&sm.done_xy);
         }
         // what is in flight ends before the block does
-        if (!on) {
-            mma_commit(&sm.tile);
-            mbar_drain(&sm.tile, 1);
-        }
+        mma_commit(&sm.drain);
+        mbar_drain(&sm.drain, 0);
         __syncwarp();
     } else if (warp == kTcWorkers / 32 + 1) {
         // ---- copies ----
-        const int all = z.group * slices;
+        const int all = chunk == a.silent ? 0 : z.group * slices;
         int q = 0;
         if (lane == 0) {
             for (; q < min(all, 2); ++q) fetch(q);
@@ -256,13 +256,15 @@ __global__ void __launch_bounds__(kTcGradThreads, 1)
                 if (!mbar_wait_one(&sm.ready[q & 1], ((q - 2) >> 1) & 1, dead)) break;
                 fetch(q);
             }
+            mbar_drain(&sm.tile, 0);
             for (int d = max(0, q - 2); d < q; ++d) mbar_drain(&sm.full[d & 1], (d >> 1) & 1);
         }
         __syncwarp();
     } else {
     const auto sync = [] { named_bar_sync(1, kTcWorkers); };
     int q = 0;  // slices so far
-    bool ok = mbar_wait(&sm.tile, 0, dead);
+    // (a wait that gives up leaves `dead` set: the outputs become NaN at the end)
+    mbar_wait(&sm.tile, 0, dead);
     for (int gh = 0; gh < z.group; ++gh) {
         const int hv = hk * z.group + gh;
         sync();  // the last head's shared values are read
@@ -289,15 +291,15 @@ __global__ void __launch_bounds__(kTcGradThreads, 1)
         for (int sl = 0; sl < slices; ++sl, ++q) {
             TcTiles<KSUB> &tl_ = sm.tiles[q & 1];
             const float(&next)[2 * 8 + 2 * Smem::kOcts][kTcCols][8] = sm.next[q & 1];
-            ok = mbar_wait(&sm.full[q & 1], (q >> 1) & 1, dead) && ok;
-            if (q >= 2) ok = mbar_wait(&sm.done[q & 1], ((q - 2) >> 1) & 1, dead) && ok;  // the tiles are read
+            mbar_wait(&sm.full[q & 1], (q >> 1) & 1, dead);
+            if (q >= 2) mbar_wait(&sm.done[q & 1], ((q - 2) >> 1) & 1, dead);  // the tiles are read
             // half a warp takes the 16 columns of eight steps of r and du
             // (warps 0-3) or of eight rows of S0 and D1 (8-15); 4-7 take GO
             const int c = lane & 15, half = lane >> 4, col = kTcCols * sl + c;
             const bool in = col < z.DV;
             if (warp < 4) {
                 // W of two slices ago has also gone out (before its readers' next arrival)
-                if (q >= 2) ok = mbar_wait(&sm.ready[(q - 1) & 1], ((q - 1) >> 1) & 1, dead) && ok;
+                if (q >= 2) mbar_wait(&sm.ready[(q - 1) & 1], ((q - 1) >> 1) & 1, dead);
                 const int oct = 2 * warp + half;
                 float x[8], y[8], dot[8];
                 load_eight(next[oct][c], in, x);
@@ -335,7 +337,7 @@ __global__ void __launch_bounds__(kTcGradThreads, 1)
             mbar_arrive(&sm.ready[q & 1]);
             if (warp >= 4 && warp < 8) {  // gv = W, transposed back
                 const int w = warp - 4;
-                ok = mbar_wait(&sm.ready[q & 1], (q >> 1) & 1, dead) && ok;
+                mbar_wait(&sm.ready[q & 1], (q >> 1) & 1, dead);
                 if (sl % 4 == 0) {  // the tile has left
                     if (warp == 4 && lane == 0) bulk_wait_read_all();
                     named_bar_sync(2, 128);
@@ -359,8 +361,8 @@ __global__ void __launch_bounds__(kTcGradThreads, 1)
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, s);
         if (lane == 0) sm.part[warp] = inner;
-        if (q >= 2) ok = mbar_wait(&sm.done[q & 1], ((q - 2) >> 1) & 1, dead) && ok;
-        ok = mbar_wait(&sm.done[(q - 1) & 1], ((q - 1) >> 1) & 1, dead) && ok;
+        if (q >= 2) mbar_wait(&sm.done[q & 1], ((q - 2) >> 1) & 1, dead);
+        mbar_wait(&sm.done[(q - 1) & 1], ((q - 1) >> 1) & 1, dead);
         tc_fence_after();
         sync();  // gv's senders have read the last W, too
         // X, -Y and P: row i of 64, columns 16 cg ..
@@ -422,7 +424,7 @@ __global__ void __launch_bounds__(kTcGradThreads, 1)
             }
             sm.sums[q][t] = s;
         }
-        ok = mbar_wait(&sm.done_xy, gh & 1, dead) && ok;
+        mbar_wait(&sm.done_xy, gh & 1, dead);
         tc_fence_after();
         // gq and gk, and their terms' products with q and k
         {
@@ -466,7 +468,6 @@ __global__ void __launch_bounds__(kTcGradThreads, 1)
         }
         tc_fence_before();
         sync();
-        ok = ok && !*dead;
         if (warp == 0) {  // two steps per lane
             float inner_sum = lane < kTcWorkers / 32 ? sm.part[lane] : 0.f;
 #pragma unroll
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(kTcGradThreads, 1)
             }
             before = __shfl_up_sync(0xffffffffu, before, 1);
             if (lane == 0) before = 0.f;
-            const float last = sm.e_last * inner_sum, nan = __int_as_float(0x7FC00000);  // where a wait gave up
+            const float last = sm.e_last * inner_sum;
             const float after = __shfl_down_sync(0xffffffffu, from, 1);
             const float reads[2] = {from, r[1] + (lane < 31 ? after : 0.f)};
             const float writes[2] = {before, before + w[0]};
@@ -500,8 +501,8 @@ __global__ void __launch_bounds__(kTcGradThreads, 1)
                 const int t = 2 * lane + e;
                 if (t >= n) continue;
                 const size_t o = (static_cast<size_t>(b) * z.T + t0 + t) * z.HV + hv;
-                a.gg[o] = ok ? last + reads[e] + writes[e] + s[e] : nan;
-                a.gbeta[o] = ok ? sm.gbeta[t] : nan;
+                a.gg[o] = last + reads[e] + writes[e] + s[e];
+                a.gbeta[o] = sm.gbeta[t];
             }
         }
     }
@@ -514,14 +515,28 @@ __global__ void __launch_bounds__(kTcGradThreads, 1)
             uint32_t o[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) o[q] = pack_bf16(acc[8 * c + 2 * q], acc[8 * c + 2 * q + 1]);
-            *reinterpret_cast<uint4 *>(p + col) = ok ? make_uint4(o[0], o[1], o[2], o[3])
-                                                     : make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+            *reinterpret_cast<uint4 *>(p + col) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
     if (warp == 4 && lane == 0) bulk_wait_all();
     }
     tc_fence_before();
     __syncthreads();
+    if (*dead) {  // a wait gave up: everything of this block becomes NaN
+        const float nan = __int_as_float(0x7FC00000);
+        for (int e = tid; e < n * z.DK; e += kTcGradThreads) {
+            const size_t o = token_offset(b, t0 + e / z.DK, hk, z.T, z.HK, z.DK) + e % z.DK;
+            from_f32(a.gq + o, nan);
+            from_f32(a.gk + o, nan);
+        }
+        // the value heads of a key head are neighbours
+        for (long long e = tid; e < static_cast<long long>(n) * z.group; e += kTcGradThreads) {
+            const size_t o = token_offset(b, t0 + static_cast<int>(e / z.group),
+                                          hk * z.group + static_cast<int>(e % z.group), z.T, z.HV, 1);
+            a.gg[o] = a.gbeta[o] = nan;
+            for (int i = 0; i < z.DV; ++i) from_f32(a.gv + o * z.DV + i, nan);
+        }
+    }
     if (warp == 0) {
         __syncwarp();
         tc_fence_after();
