@@ -1,5 +1,5 @@
 """The gated delta rule where its answers are easily a little or wholly off:
-roundings of bf16 outputs, sizes of 0.
+roundings of bf16 outputs, sizes of 0, the ends of its buffers.
 
 The oracle is the float64 step-by-step one; it is fed the rounded inputs.
 """
@@ -82,3 +82,78 @@ def test_sums_over_nothing_are_zero(m, shape, dtype):
     grads = m.gated_delta_backward(*(x[n] for n in INPUTS), x["go"], s_in=x["s_in"], gs_out=x["gs_out"])
     for name, gr in zip(INPUTS + ("s_in",), grads):
         assert gr.shape == x[name].shape and (gr == 0).all(), name
+
+
+GUARD = 1024     # bytes around every buffer
+
+
+class Guarded:
+    """Buffers of exact sizes with guard bands, filled with 0xFF (NaN in every
+    type): what a call leaves unwritten or reads before writing shows."""
+
+    def __init__(self):
+        self.bufs = []
+
+    def __call__(self, nbytes):
+        buf = torch.full((nbytes + 2 * GUARD,), 0xFF, dtype=torch.uint8, device="cuda")
+        self.bufs.append(buf)
+        return buf[GUARD:GUARD + nbytes]
+
+    def like(self, t):
+        return self(t.numel() * t.element_size()).view(t.dtype).view(t.shape)
+
+    def check(self):
+        for i, buf in enumerate(self.bufs):
+            assert (buf[:GUARD] == 0xFF).all() and (buf[-GUARD:] == 0xFF).all(), f"buffer {i}"
+
+
+TOL32, TOL16 = 2e-5, 1.5 * 2.0 ** -8     # as in test_gpu_delta.py
+
+
+def assert_near(got, want, what):
+    tol = TOL16 if got.dtype == torch.bfloat16 else TOL32
+    got = host(got)
+    assert np.isfinite(got).all(), what
+    assert np.linalg.norm(got - want) <= tol * np.linalg.norm(want) + 1e-30, what
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 1, 1, 2, 64, 64), (2, 70, 1, 3, 64, 40), (1, 129, 1, 2, 128, 72), (2, 130, 2, 2, 72, 104),
+                                   (1, 63, 1, 2, 33, 17), (1, 150, 1, 1, 8, 8), (1, 200, 1, 2, 24, 128)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_outputs_and_scratch_stay_in_bounds(m, shape, dtype):
+    """Every output and a scratch of the size asked for, through the C entry
+    points: nothing around them changes, nothing in them is left out, and what
+    the scratch held does not matter."""
+    x = draw(*shape, dtype=dtype, seed=sum(shape))
+    sizes, es = shape, x["q"].element_size()
+    B, T, HK, HV, DK, DV = shape
+    suffix, scale = ("" if dtype == "f32" else "_bf16"), DK ** -0.5
+    p = {n: t.data_ptr() for n, t in x.items()}
+    ins = [p[n] for n in INPUTS]
+    stream = torch.cuda.current_stream().cuda_stream
+    for with_state in (False, True):
+        mem = Guarded()
+        o, s_out = mem.like(x["v"]), mem.like(x["s_in"])
+        n = m.lib.gated_delta_scratch(B, T, HV, DK, DV, es, with_state)
+        st = getattr(m.lib, "gated_delta" + suffix)(*sizes, *ins, scale, o.data_ptr(), p["s_in"],
+                                                    s_out.data_ptr() if with_state else None,
+                                                    mem(n).data_ptr() if n else None, n, stream)
+        assert st == m.WKV_OK, m.wkv_last_error()
+        want, ws = od.gated_delta(*(host(x[i]) for i in INPUTS), scale, host(x["s_in"]))
+        assert_near(o, want, "o")
+        if with_state:
+            assert_near(s_out, ws, "s_out")
+        mem.check()
+    mem = Guarded()
+    outs = {n: mem.like(x[n]) for n in INPUTS + ("s_in",)}
+    n = m.lib.gated_delta_backward_scratch(B, T, HV, DK, DV, es)
+    st = getattr(m.lib, "gated_delta_backward" + suffix)(
+        *sizes, *ins, scale, p["s_in"], p["go"], p["gs_out"], *(t.data_ptr() for t in outs.values()),
+        mem(n).data_ptr(), n, stream)
+    assert st == m.WKV_OK, m.wkv_last_error()
+    want = od.gated_delta_backward(*(host(x[i]) for i in INPUTS), scale, host(x["go"]), host(x["s_in"]),
+                                   host(x["gs_out"]))
+    for (name, t), w in zip(outs.items(), want):
+        assert_near(t, w, name)
+    mem.check()
