@@ -121,12 +121,16 @@ def _empty(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _empty_like(t, stream):
+def _empty_like_on(stream):
+    """torch.empty_like in the same way: torch's own where no stream is given."""
     import torch
     if stream is None:
-        return torch.empty_like(t)
-    with torch.cuda.stream(stream):
-        return torch.empty_like(t)
+        return torch.empty_like
+
+    def make(t):
+        with torch.cuda.stream(stream):
+            return torch.empty_like(t)
+    return make
 
 
 def _need(t, name, dtype, ndim):
@@ -155,7 +159,7 @@ def _wkv(fn_name, io_dtype, w, u, k, v, y, stream):
     if w.shape[0] != C or u.shape[0] != C:
         raise ValueError("w and u must be [C]")
     if y is None:
-        y = _empty_like(k, stream)
+        y = _empty_like_on(stream)(k)
     else:
         _need(y, "y", io_dtype, 3)
         if y.shape != k.shape:
@@ -196,7 +200,7 @@ def _wkv_state(fn_name, io_dtype, w, u, k, v, s_in, y, s_out, stream):
     if w.shape[0] != C or u.shape[0] != C:
         raise ValueError("w and u must be [C]")
     if y is None:
-        y = _empty_like(k, stream)
+        y = _empty_like_on(stream)(k)
     else:
         _need(y, "y", io_dtype, 3)
         if y.shape != k.shape:
@@ -248,7 +252,7 @@ def wkv_forward_gated(w, u, k, v, r, y=None, s_in=None, s_out=None, stream=None)
             if tuple(t.shape) != (B, 3, C):
                 raise ValueError(f"{name} must be [B, 3, C] = {(B, 3, C)}")
     if y is None:
-        y = _empty_like(k, stream)
+        y = _empty_like_on(stream)(k)
     else:
         _need(y, "y", io, 3)
         if y.shape != k.shape:
@@ -322,7 +326,7 @@ def diag_scan(a, b, h0=None, h=None, stream=None):
         if tuple(h0.shape) != (B, D):
             raise ValueError("h0 must be [B, D]")
     if h is None:
-        h = _empty_like(a, stream)
+        h = _empty_like_on(stream)(a)
     else:
         _need(h, "h", io, 3)
         if h.shape != a.shape:
@@ -347,8 +351,8 @@ def wkv_backward(w, u, k, v, gy, stream=None):
     B, T, C = k.shape
     if w.shape[0] != C or u.shape[0] != C:
         raise ValueError("w and u must be [C]")
-    gk, gv = _empty_like(k, stream), _empty_like(k, stream)
-    gw, gu = _empty_like(w, stream), _empty_like(u, stream)
+    new = _empty_like_on(stream)
+    gk, gv, gw, gu = new(k), new(k), new(w), new(u)
     _check(lib.wkv_backward(B, T, C, w.data_ptr(), u.data_ptr(), k.data_ptr(), v.data_ptr(),
                             gy.data_ptr(), gk.data_ptr(), gv.data_ptr(), gw.data_ptr(),
                             gu.data_ptr(), _stream_handle(stream)), "wkv_backward")
@@ -379,7 +383,7 @@ def lru_scan(nu_log, theta_log, u, gamma=None, x0=None, x=None, stream=None):
         if tuple(x0r.shape) != (B, D, 2):
             raise ValueError("x0 must be [B, D] complex")
     if x is None:
-        x = _empty_like(u, stream)
+        x = _empty_like_on(stream)(u)
     xr = torch.view_as_real(x) if x.dtype == torch.complex64 else x
     _need(xr, "x", torch.float32, 4)
     if xr.shape != ur.shape:
@@ -455,7 +459,7 @@ def gated_delta(q, k, v, g, beta, scale=None, s_in=None, o=None, s_out=None, str
         if t is not None:
             _tensor(t, name, torch.float32, (B, HV, DK, DV))
     if o is None:
-        o = torch.empty_like(v) if stream is None else _empty_like(v, stream)
+        o = torch.empty_like(v) if stream is None else _empty_like_on(stream)(v)
     else:
         _tensor(o, "o", io, v.shape)
     fn = "gated_delta" if io == torch.float32 else "gated_delta_bf16"
@@ -480,9 +484,9 @@ def gated_delta_backward(q, k, v, g, beta, go, scale=None, s_in=None, gs_out=Non
     for t, name in ((s_in, "s_in"), (gs_out, "gs_out")):
         if t is not None:
             _tensor(t, name, torch.float32, (B, HV, DK, DV))
-    gq, gk, gv = _empty_like(q, stream), _empty_like(k, stream), _empty_like(v, stream)
-    gg, gbeta = _empty_like(g, stream), _empty_like(beta, stream)
-    gs_in = None if s_in is None else _empty_like(s_in, stream)
+    new = _empty_like_on(stream)
+    gq, gk, gv, gg, gbeta = new(q), new(k), new(v), new(g), new(beta)
+    gs_in = None if s_in is None else new(s_in)
     n = lib.gated_delta_backward_scratch(B, T, HV, DK, DV, q.element_size())
     scratch = _scratch(n, q, stream)
     fn = "gated_delta_backward" if io == torch.float32 else "gated_delta_backward_bf16"
@@ -527,7 +531,7 @@ def group_norm(x, groups, weight=None, bias=None, gate=None, act="none", eps=1e-
     import torch
     io, N, C, code = _norm_sizes(x, groups, weight, bias, gate, act)
     if y is None:
-        y = torch.empty_like(x) if stream is None else _empty_like(x, stream)
+        y = torch.empty_like(x) if stream is None else _empty_like_on(stream)(x)
     else:
         _tensor(y, "y", io, x.shape)
     fn = "group_norm" if io == torch.float32 else "group_norm_bf16"
@@ -543,10 +547,11 @@ def group_norm_backward(x, gy, groups, weight=None, bias=None, gate=None, act="n
     import torch
     io, N, C, code = _norm_sizes(x, groups, weight, bias, gate, act)
     _tensor(gy, "gy", io, x.shape)
-    gx = _empty_like(x, stream)
-    gweight = None if weight is None else _empty_like(weight, stream)
-    gbias = None if bias is None else _empty_like(bias, stream)
-    ggate = None if gate is None else _empty_like(gate, stream)
+    new = _empty_like_on(stream)
+    gx = new(x)
+    gweight = None if weight is None else new(weight)
+    gbias = None if bias is None else new(bias)
+    ggate = None if gate is None else new(gate)
     n = lib.group_norm_backward_scratch(N, C)
     scratch = _scratch(n, x, stream)
     fn = "group_norm_backward" if io == torch.float32 else "group_norm_backward_bf16"
