@@ -94,6 +94,10 @@ wkv_status with_shape(const DeltaSizes &z, int sms, const Launch &launch) {
     return launched();
 }
 
+// A lane holds 8, 12 or 16 rows of the state, for heads of at most 64, 96 and 128
+// rows.  (What 12 save against 16: one token of 512 heads of 96 x 96 10.1 against
+// 11.1 us, 24 steps of 256 heads in bf16 22.6 against 27.4, 400 in fp32 287
+// against 352.)
 template <typename IO>
 wkv_status launch_recurrent(const DeltaFwdArgs<IO> &a, int sms, cudaStream_t s) {
     return with_shape<IO>(a.z, sms, [&](auto nw, auto cpl) {
@@ -147,13 +151,19 @@ bool chunked_fits(const DeltaSizes &z, const void *q, const void *k, const void 
 }
 
 // The forward does from some steps on: its two launches cost a few tens of
-// steps.  4 heads of 64, chunked against step by step: 15 and 14 us at 24
-// steps, 15 and 19 at 33; 32 heads of 128: 20 and 15, 20 and 19, 20 and 25 at
-// 48; with more heads than SMs a chunk's latency counts several times, 512
-// heads of 64: 44 and 36 at 48, 41 and 46 at 64.  The gradient does at once: 34
-// against 47 us at 17 steps of 4 heads of 64, 46 against 89 with 32 of 128.
+// steps.  Up to as many heads as SMs, chunked against step by step: 4 heads of
+// 64, 16 and 14 us at 24 steps, 16 and 19 at 33; 32 heads of 128, 20 and 15, 20
+// and 20, and 20 and 25 at 48.  With more heads a chunk's latency counts several
+// times, the steps' too where a state is wide: 512 heads of 128, 65 and 66 us at
+// 33 steps, 68 and 103 at 56; of 72 x 104, 53 and 53 at 33.  States of at most 64
+// columns go on step by step for longer: 256 heads of 64, 27 and 28 at 48 steps;
+// 512 heads, 43 and 36 at 48, 40 and 47 at 64; of 128 x 64, 55 and 58 at 56.
+//
+// The gradient does at any length: 34 against 39 us at one step of 4 heads of
+// 64, 44 against 80 of 32 heads of 128, 421 against 521 of 2048 heads of 64 (41
+// against 40 of 128 heads of 64 is the worst), and the more the longer.
 bool chunked_forward(int64_t B, int64_t T, int64_t HV, int64_t DK, int64_t DV, int elem_bytes) {
-    return T > (B * HV <= 148 ? 32 : 56) && chunked_sizes(T, HV, DK, DV, elem_bytes);
+    return T > (B * HV <= 148 || DV > 64 ? 32 : 56) && chunked_sizes(T, HV, DK, DV, elem_bytes);
 }
 
 size_t chunk_count(int64_t T) { return static_cast<size_t>((T + kDeltaChunk - 1) / kDeltaChunk); }

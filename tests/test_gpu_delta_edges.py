@@ -157,3 +157,18 @@ def test_outputs_and_scratch_stay_in_bounds(m, shape, dtype):
     for (name, t), w in zip(outs.items(), want):
         assert_near(t, w, name)
     mem.check()
+
+
+@pytest.mark.parametrize("shape", [(8, 33, 4, 32, 64, 72), (8, 56, 8, 32, 64, 64), (8, 57, 8, 32, 64, 64), (5, 32, 10, 30, 72, 104)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_more_heads_than_sms_around_the_chunked_lengths(m, shape):
+    """Both sides of the lengths from which bf16 calls of many heads take the
+    chunked kernels: wide states from 33 steps on, others from 57."""
+    B, T, HK, HV, DK, DV = shape
+    x = draw(*shape, dtype="bf16", seed=sum(shape))
+    assert (m.lib.gated_delta_scratch(B, T, HV, DK, DV, 2, 1) > 0) == (T > (32 if DV > 64 else 56))
+    s_out = torch.empty_like(x["s_in"])
+    o = m.gated_delta(*(x[n] for n in INPUTS), s_in=x["s_in"], s_out=s_out)
+    want, ws = od.gated_delta(*(host(x[n]) for n in INPUTS), DK ** -0.5, host(x["s_in"]))
+    assert_near(o, want, "o")
+    assert_near(s_out, ws, "s_out")
