@@ -41,6 +41,7 @@ inline wkv_status cuda_fail(cudaError_t e, const char *what) {
 struct Driver {
     PFN_cuTensorMapEncodeTiled_v12000 encode_tiled = nullptr;
     PFN_cuMemGetAddressRange_v3020 get_address_range = nullptr;
+    PFN_cuPointerGetAttribute_v4000 get_attribute = nullptr;
 };
 
 inline const Driver &driver() {
@@ -58,9 +59,40 @@ inline const Driver &driver() {
                 cudaSuccess &&
             q == cudaDriverEntryPointSuccess)
             d.get_address_range = reinterpret_cast<PFN_cuMemGetAddressRange_v3020>(p);
+        p = nullptr;
+        if (cudaGetDriverEntryPoint("cuPointerGetAttribute", &p, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            d.get_attribute = reinterpret_cast<PFN_cuPointerGetAttribute_v4000>(p);
         cudaGetLastError();
     });
     return d;
+}
+
+// Whether an address lies in memory that its owner maps into an address range
+// piece by piece (a growing segment of an allocator, say): neither cudaMalloc's
+// (which older inter-process handles can share) nor a memory pool's.
+inline bool mapped_by_pieces(const Driver &d, CUdeviceptr p) {
+    if (d.get_attribute == nullptr) return false;
+    int shareable = 1;
+    CUmemoryPool pool = nullptr;
+    return d.get_attribute(&shareable, CU_POINTER_ATTRIBUTE_IS_LEGACY_CUDA_IPC_CAPABLE, p) == CUDA_SUCCESS &&
+           d.get_attribute(&pool, CU_POINTER_ATTRIBUTE_MEMPOOL_HANDLE, p) == CUDA_SUCCESS && shareable == 0 &&
+           pool == nullptr;
+}
+
+// The first address behind p's allocation, 0 if it is not known.  Pieces that
+// follow one another without a gap are one allocation, as far as `enough`.
+inline uintptr_t allocation_end(const Driver &d, CUdeviceptr p, uintptr_t enough) {
+    CUdeviceptr base = 0;
+    size_t size = 0;
+    if (d.get_address_range == nullptr || d.get_address_range(&base, &size, p) != CUDA_SUCCESS) return 0;
+    uintptr_t end = static_cast<uintptr_t>(base) + size;
+    while (end < enough && mapped_by_pieces(d, end - 1) &&
+           d.get_address_range(&base, &size, end) == CUDA_SUCCESS && base == end && size > 0 &&
+           mapped_by_pieces(d, end))
+        end += size;
+    return end;
 }
 
 // One pointer argument: its extent in bytes, whether it may be NULL, and
@@ -93,19 +125,11 @@ inline wkv_status check_buffer(const Buf &b, int dev) {
     if (attr.type == cudaMemoryTypeDevice && attr.device != dev)
         return fail(WKV_ERR_INVALID_ARG, "%s lives on device %d, current device is %d", b.name,
                     attr.device, dev);
-    const Driver &d = driver();
-    if (d.get_address_range != nullptr) {
-        CUdeviceptr base = 0;
-        size_t size = 0;
-        if (d.get_address_range(&base, &size, reinterpret_cast<CUdeviceptr>(b.p)) == CUDA_SUCCESS) {
-            const uintptr_t end = static_cast<uintptr_t>(base) + size;
-            if (reinterpret_cast<uintptr_t>(b.p) + b.bytes > end)
-                return fail(WKV_ERR_INVALID_ARG,
-                            "%s: %zu bytes needed but its allocation ends %zu bytes after it",
-                            b.name, b.bytes,
-                            static_cast<size_t>(end - reinterpret_cast<uintptr_t>(b.p)));
-        }
-    }
+    const uintptr_t p = reinterpret_cast<uintptr_t>(b.p);
+    const uintptr_t end = allocation_end(driver(), p, p + b.bytes);
+    if (end != 0 && p + b.bytes > end)
+        return fail(WKV_ERR_INVALID_ARG, "%s: %zu bytes needed but its allocation ends %zu bytes after it", b.name,
+                    b.bytes, static_cast<size_t>(end - p));
     return WKV_OK;
 }
 
