@@ -23,7 +23,8 @@
 //   bf16 operand tiles in scratch memory, laid out as the chain's shared
 //   memory wants them.
 //
-//   delta_chain_kernel, one block per head: only the products with the state
+//   delta_chain(), one block per head (the kernels delta_forward_kernel and
+//   delta_sweeps_kernel): only the products with the state
 //   and what depends on them:
 //
 //       P = S0^T K^T;  x = V^T T^T + (a P) T^T;  S1 = e S0 + (b x)^T K

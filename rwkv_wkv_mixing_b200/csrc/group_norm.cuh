@@ -90,9 +90,14 @@ struct NormVec<__nv_bfloat16, 8> {
 };
 
 // e^-z and p = 1 / (1 + e^-z).  With bf16 I/O by the hardware's exponential
-// and reciprocal (a few 2^-22 of the value, 2^-9 is what the output keeps):
-// two instructions instead of about thirty, without which the arithmetic and
-// not the memory is the bound.
+// and reciprocal: two instructions instead of about thirty, without which the
+// arithmetic and not the memory is the bound.  e is off by some 2^-22 plus
+// |z| 2^-24 of itself (the rounding of the exponential's argument): 2^-22 around
+// 0, 2^-17 at |z| = 80.  Of p that is less: next to 1, e is small, and next to 0 p
+// and what it multiplies are.  The outputs keep 2^-9, and gweight and gbias, fp32
+// sums of such terms, weigh each by the activation it belongs to.  For fp32 by
+// expf and the fast division (2 units in the last place; from z = -87.3 down
+// p is 0 instead of 2^-126 and less).
 template <typename IO>
 __device__ __forceinline__ float norm_sigmoid(float z, float &e) {
     if constexpr (sizeof(IO) == 2) {

@@ -53,20 +53,6 @@ __device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity) {
     while (!mbar_try_wait(bar, parity) && global_timer_ns() - start < kWaitLimitNs) {}
 }
 
-// Named barrier over nthreads threads; true in all of them if `ok` was in all.
-__device__ __forceinline__ bool named_bar_all(int id, int nthreads, bool ok) {
-    int all;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.s32 p, %1, 0;\n\t"
-        "barrier.cta.red.and.pred q, %2, %3, p;\n\t"
-        "selp.s32 %0, 1, 0, q;\n\t}"
-        : "=r"(all)
-        : "r"(ok ? 1 : 0), "r"(id), "r"(nthreads)
-        : "memory");
-    return all != 0;
-}
-
 // this thread's warp, as a value that the compiler knows to be the same in all
 // of its lanes
 __device__ __forceinline__ int warp_index() {
