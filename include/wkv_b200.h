@@ -292,12 +292,19 @@ WKV_API wkv_status diag_scan_bf16(int64_t B, int64_t T, int64_t D,
  * s_in NULL = zeros; s_out NULL: no state out; s_out may be s_in (update in
  * place), any other overlap of an output is WKV_ERR_INVALID_ARG.  T = 0 only
  * copies the state (or zeros) to s_out.  T = 1 is one decoding step.
- * The state and every sum are fp32, whatever the I/O type.
+ * The state and every sum are fp32, whatever the I/O type.  bf16 calls that
+ * take 64 steps at a time keep the operands of their products that are not
+ * inputs (the state, residuals, products of keys and queries) as sums of bf16
+ * parts: of all 24 bits in what reaches s_out, of 16 bits in what reaches only
+ * o -- all of it when s_out is NULL, so that o may differ in the last bit of a
+ * few elements from the same call with s_out.  Either way o is the rounding of a
+ * value that is off by some 2^-16 of its terms' size.
  * `scratch`: caller's device memory, 16-byte aligned, at least
- * gated_delta_scratch() bytes (0 for single tokens, short calls and fp32: it
- * may be NULL then; at most about 660 bytes per step and value head), free to
- * use again once the call's work on the stream is done; its contents do not
- * matter.  Calls that may run at the same time, replays of captured graphs
+ * gated_delta_scratch() bytes, free to use again once the call's work on the
+ * stream is done; its contents do not matter.  That is, for bf16 calls that
+ * take 64 steps at a time (from 33 steps on, or 57 with more heads than SMs of
+ * at most 64 columns; DK and DV multiples of 8), 33792 bytes per value head and
+ * started chunk of 64 steps, 41984 with s_out; 0 (it may be NULL) for others.  Calls that may run at the same time, replays of captured graphs
  * among them, need a scratch each.  elem_bytes: 2 for the bf16 call, 4 for
  * fp32; with_state: whether s_out is given.
  * A device-side wait that gives up (of these calls and their gradients) leaves
@@ -328,10 +335,13 @@ WKV_API wkv_status gated_delta_bf16(int64_t B, int64_t T, int64_t HK, int64_t HV
  *     gk_t = beta_t D_t r_t - S'_t w_t,  gg_t = <D_t - k_t w_t^T, S'_t>.
  *
  * Recomputes the states from the inputs.  `scratch`: caller's device memory,
- * 16-byte aligned, at least gated_delta_backward_scratch() bytes (per
- * step and value head about DK DV / 8 + 8 DV, for bf16 another 1550 to 1950,
- * for fp32 8 DK), under the same rules as gated_delta's.  No output may overlap an input or another output.  T = 0:
- * gs_in = gs_out (or zeros).  Deterministic: repeated calls give the same
+ * 16-byte aligned, at least gated_delta_backward_scratch() bytes, under the
+ * same rules as gated_delta's.  That is, with T and DV rounded up to multiples
+ * of 64 and 16, per value head and chunk of 64 steps 8 DV (DK + 64) bytes and,
+ * for bf16 with DK and DV multiples of 8, another 100352 (DK up to 64) or
+ * 124928, for others 8 DK a step (of T as it is); and up to 1 KB for alignment.
+ * No output may overlap an input or another output.  T = 0: gs_in = gs_out (or
+ * zeros).  Deterministic: repeated calls give the same
  * bits. */
 WKV_API int64_t gated_delta_backward_scratch(int64_t B, int64_t T, int64_t HV, int64_t DK,
                                              int64_t DV, int elem_bytes);
