@@ -172,3 +172,24 @@ def test_more_heads_than_sms_around_the_chunked_lengths(m, shape):
     want, ws = od.gated_delta(*(host(x[n]) for n in INPUTS), DK ** -0.5, host(x["s_in"]))
     assert_near(o, want, "o")
     assert_near(s_out, ws, "s_out")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 150, 2, 4, 64, 64), (2, 70, 1, 2, 128, 128), (2, 90, 1, 3, 40, 24)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_nan_in_a_gradient_stays_in_its_row_and_head(m, shape, dtype):
+    """A NaN in one value head's v: the gradients of the other rows and of the
+    other heads' own tensors have the bits they have without it; gq and gk sum
+    over the value heads of a key head, the other key heads' stay too."""
+    x = draw(*shape, dtype=dtype, seed=sum(shape))
+    HK, HV = shape[2:4]
+    run = lambda: m.gated_delta_backward(*(x[n] for n in INPUTS), x["go"], s_in=x["s_in"], gs_out=x["gs_out"])  # noqa: E731
+    want = [t.clone() for t in run()]
+    x["v"][0, 40, 1, 3] = float("nan")
+    for name, got, w in zip(INPUTS + ("s_in",), run(), want):
+        assert torch.equal(got[1], w[1]), name
+        head = 1 // (HV // HK) if name in ("q", "k") else 1
+        axis = 0 if name == "s_in" else 1     # of got[0]
+        rest = [h for h in range(got[0].shape[axis]) if h != head]
+        idx = torch.tensor(rest, dtype=torch.int64, device="cuda")
+        assert torch.equal(got[0].index_select(axis, idx), w[0].index_select(axis, idx)), name
