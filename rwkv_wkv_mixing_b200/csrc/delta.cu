@@ -60,8 +60,8 @@ DeltaSizes sizes(int64_t B, int64_t T, int64_t HK, int64_t HV, int64_t DK, int64
 // sub-partitions, one-warp blocks spread them over more SMs (the staged rows
 // then come from L2 several times).  Long fp32 sequences take warps of a
 // quarter of the columns as long as these are few enough not to wait for one
-// another: B=3 T=777, 6 heads of 96 x 80 181 against 305 us; B=4 T=2048, 8
-// heads of 128 530 against 799 us.  (A few steps are bound by the state's
+// another: B=3 T=777, 6 heads of 96 x 80 166 against 284 us; B=4 T=2048, 8
+// heads of 128 545 against 816 us.  (A few steps are bound by the state's
 // loads, whose rows would be 16 bytes wide.)
 enum class RecShape { kWide, kOne, kNarrow, kNarrowFour };
 

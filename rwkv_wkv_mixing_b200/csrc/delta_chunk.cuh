@@ -52,16 +52,16 @@
 // parts (16 bits, three pairs) where only o does, and in what reaches nothing
 // but o: S in Q S0, M and r in M r.  16 bits leave the value that is rounded
 // to o within 2^-16 of its terms' size, so that o is the rounding of the exact
-// value but for one step in some 500 (with M in one part its error was 1.4
-// times the rounding's).
+// value for all but one element in some 300 (with M in one part its error was
+// 1.3 to 1.4 times the rounding's).
 //
 // Bound: the chain of three dependent products per chunk with the loads and
-// conversions between them, not bandwidth: 4100 cycles with 64 columns in two
-// parts, 7900 with 128 in three, of which the tensor cores work 1400 and 3000.
-// B=8 T=4096, 40 heads of 64: preparation 267 us, chain 534 us; B=1 T=16384, 32
-// heads of 128 with the state: 177 and 1150 us (step by step: 3932 and 21924 in
-// all).  Both sweeps of B=2 T=4096, 32 heads of 128: 360 us, their 870 MB of
-// stores about half of it.
+// conversions between them, not bandwidth: 5200 cycles with 64 columns in two
+// parts, 8100 with 128 in three, of which the tensor cores work 1500 and 3200.
+// B=8 T=4096, 40 heads of 64: preparation 264 us, chain 540 us; B=1 T=16384, 32
+// heads of 128 with the state: 154 and 1040 us (step by step: 3932 and 21924 in
+// all).  Both sweeps of B=2 T=4096, 32 heads of 128: 303 us, for 870 MB of
+// stores.
 #pragma once
 
 #include "delta_common.cuh"

@@ -24,11 +24,11 @@
 // out from the operand itself (its first part is the rounded value), 64 columns
 // at a time.
 //
-// Bound: about 32000 cycles a head and chunk with DK = DV = 128, two thirds the
+// Bound: about 30000 cycles a head and chunk with DK = DV = 128, two thirds the
 // eight slices' conversions (1300 cycles) and products (1100), which wait for
-// one another, one third the read-out; 31 % of the issue slots, 24 % of the
-// tensor cores.  B=2 T=4096, 32 heads of 128: 533 us (fp32 multiply-adds: 2140);
-// B=8 T=1024, 12 heads of 64: 147 us (633).
+// one another, one third the read-out; 30 % of the issue slots, 25 % of the
+// tensor cores.  B=2 T=4096, 32 heads of 128: 498 us (fp32 multiply-adds: 2140);
+// B=8 T=1024, 12 heads of 64: 142 us (633).
 #pragma once
 
 #include "delta_chunk.cuh"

@@ -26,7 +26,7 @@
 // step's sums and exchanges, and with many heads by the three multiply-adds
 // per element, 3 DK DV / 128 cycles of an SM per step and head.  256 rows' next
 // tokens, 32 heads of 128: 176 us, 6.1 TB/s; one row's: 4.7 us.  fp32 T=777, 18
-// heads of 96 x 80: 168 us, 0.22 us a step.
+// heads of 96 x 80: 166 us, 0.21 us a step.
 #pragma once
 
 #include "delta_common.cuh"
